@@ -430,10 +430,10 @@ def preference_loss(logits: torch.Tensor, ids: torch.Tensor, offsets: torch.Tens
     Sequence i < P is preferred over sequence P + i.  With R_s the sum (or with
     length_average the mean) of logp - ref_logp over a sequence's valid tokens,
     u = beta (R_i - R_{P+i}) - margin_i and pair_loss is, by ``kind``,
-    "sigmoid" -log sigmoid(u) (with label_smoothing), "hinge" max(0, 1 - u) or
-    "squared" (u / beta - 1 / (2 beta))^2.  loss = sum(weights * pair_loss),
-    weights defaulting to 1/P; reward = beta R.  The gradient flows from
-    ``loss`` to ``logits`` only.
+    "sigmoid" -log sigmoid(u) (with label_smoothing, which the others ignore),
+    "hinge" max(0, 1 - u) or "squared" (u / beta - 1 / (2 beta))^2.
+    loss = sum(weights * pair_loss), weights defaulting to 1/P; reward = beta R.
+    The gradient flows from ``loss`` to ``logits`` only.
     """
     n, lead = logits.shape[:-1].numel(), logits.shape[:-1]
     ids2 = _loss_ids(ids, logits, n, None)

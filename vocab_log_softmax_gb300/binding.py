@@ -570,6 +570,16 @@ def _loss_out(device, written: bool, *shapes) -> list:
     return [make(shape, dtype=torch.float32, device=device) for shape in shapes]
 
 
+def _pref_cfg(kind: str, length_average: bool, beta: float, label_smoothing: float):
+    """vls_pref_cfg of a preference loss.  Label smoothing belongs to the sigmoid
+    loss; the others take a valid value and have none."""
+    if kind not in _PREF:
+        raise ValueError(f"kind must be one of {sorted(_PREF)}")
+    if kind != "sigmoid" and 0.0 <= label_smoothing < 0.5:
+        label_smoothing = 0.0
+    return _lib.VlsPrefCfg(_PREF[kind], 1 if length_average else 0, beta, label_smoothing)
+
+
 def vls_policy_loss(logits: torch.Tensor, ids: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
                     weights: torch.Tensor | None = None, ref_logp: torch.Tensor | None = None, *,
                     clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0, kl_coef: float = 0.0,
@@ -626,15 +636,15 @@ def vls_preference_loss(logits: torch.Tensor, ids: torch.Tensor, offsets: torch.
                         margin: torch.Tensor | None = None, *, kind: str = "sigmoid", beta: float = 0.1,
                         label_smoothing: float = 0.0, length_average: bool = False, ignore_index: int = -100,
                         cap: float = 0.0, grad: bool = True, dlogits=None, stream=None) -> dict:
-    """Preference loss of P pairs among 2 P sequences (offsets [2 P + 1]).
-    Returns 'loss' (scalar), 'pair_loss' [P], 'reward' [2 P], 'logp' and
-    'coef' [N], 'stats' [N, 2] and 'dlogits' [N, V] (None without grad)."""
+    """Preference loss of P pairs among 2 P sequences (offsets [2 P + 1]);
+    label_smoothing acts on kind "sigmoid" only.  Returns 'loss' (scalar),
+    'pair_loss' [P], 'reward' [2 P], 'logp' and 'coef' [N], 'stats' [N, 2] and
+    'dlogits' [N, V] (None without grad)."""
     lib = _lib.load()
     n, v, lay = _rows(logits)
     dt, dev = _dtype(logits), logits.device
     ids = _ids64(ids, n, 1, dev)
-    if kind not in _PREF:
-        raise ValueError(f"kind must be one of {sorted(_PREF)}")
+    cfg = _pref_cfg(kind, length_average, beta, label_smoothing)
     if offsets.numel() % 2 == 0:
         raise ValueError("offsets must have 2 P + 1 elements")
     offsets = _ids64(offsets, offsets.numel(), 1, dev)
@@ -644,8 +654,7 @@ def vls_preference_loss(logits: torch.Tensor, ids: torch.Tensor, offsets: torch.
     d = _grad_out(dlogits, grad, n, v, logits)
     loss, pair_loss, reward, logp, coef, stats = _loss_out(dev, pairs > 0, (), pairs, 2 * pairs, n, n, (n, 2))
     st = lib.vls_preference_loss(logits.data_ptr(), lay, dt, n, v, ids.data_ptr(), ignore_index, cap, offsets.data_ptr(),
-                                 pairs, _lib.VlsPrefCfg(_PREF[kind], 1 if length_average else 0, beta, label_smoothing),
-                                 p_ref, p_mar, p_w, loss.data_ptr(), pair_loss.data_ptr(), reward.data_ptr(),
+                                 pairs, cfg, p_ref, p_mar, p_w, loss.data_ptr(), pair_loss.data_ptr(), reward.data_ptr(),
                                  logp.data_ptr(), coef.data_ptr(), stats.data_ptr(), _ptr(d), _raw_stream(dev, stream))
     _lib.check("vls_preference_loss", st)
     return {"loss": loss, "pair_loss": pair_loss, "reward": reward, "logp": logp, "coef": coef, "stats": stats,
