@@ -310,8 +310,7 @@ def run(st):
                                temperature=c["temperature"])
         return {key: o[key] for key in ("loss", "row_loss", "dlogits")}
     o = B.vls_preference_loss(st["logits"], st["ids"], st["offsets"], st["ref"], st["weights"], kind=c["kind"], beta=0.1,
-                              label_smoothing=c["smoothing"] if c["kind"] == "sigmoid" else 0.0,
-                              length_average=c["average"], cap=c["cap"])
+                              label_smoothing=c["smoothing"], length_average=c["average"], cap=c["cap"])
     return {key: o[key] for key in ("loss", "pair_loss", "reward", "logp", "dlogits")}
 
 
