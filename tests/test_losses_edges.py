@@ -50,3 +50,55 @@ def test_label_smoothing_reaches_the_sigmoid_loss_alone():
         assert (cfg.kind, cfg.length_average, cfg.beta) == (code, 1, 0.25)
         assert cfg.label_smoothing == (0.125 if kind == "sigmoid" else 0.0)
         assert B._pref_cfg(kind, False, 0.25, 0.5).label_smoothing == 0.5      # for the library to refuse
+
+
+# ---------------------------------------------------------------------------
+# distillation: large teacher logits under a temperature
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("lse", [False, True])
+@pytest.mark.parametrize("k", [16, 64, 65, 300])
+@pytest.mark.parametrize("tau", [float(np.float32(0.7)), 1.5])
+@pytest.mark.parametrize("offset", [0.0, 100.0, 1000.0, -8192.0])
+def test_teacher_offset_under_a_temperature(offset, tau, k, lse):
+    """A common offset of the teacher's logits moves no probability by more than
+    the rounding of their differences: those are multiples of 1/64 below 32, so
+    exact in fp32, and their scaling by 1/tau is off by 2^-23 of at most 32 / 0.7
+    (6e-6 at an exponent of 46, whose probability is below 1e-20; 2e-6 at the
+    exponents of up to 15 that matter).  With the teacher's log-sum-exp the
+    largest logit's gap to it is one rounded difference, of a few units."""
+    gen = _gen(k)
+    x = _logits(4, 5000, "fp32", gen)
+    ids, t, w, _ = _distill_inputs(x, k, gen, distinct=True)
+    t = (t * 64).round() / 64 + offset
+    ls = None
+    if lse:
+        more = torch.tensor([0.1, 0.7, 1.3, 2.1], dtype=torch.float64, device=DEV)
+        ls = (torch.logsumexp(t.double() / tau, 1) + more).float()
+    out = B.vls_distill_loss(x, ids, t, w, ls, temperature=tau)
+    _check_distill(x, ids, t, w, ls, out, tau=tau, what=f"offset {offset}")
+
+
+@gpu
+@pytest.mark.parametrize("lse", [False, True])
+def test_teacher_rows_without_mass(lse):
+    """Teacher entries that are all -inf: without the log-sum-exp they have no
+    distribution (NaN); with it every probability is 0, and so are the loss and
+    the gradient."""
+    gen = _gen(14)
+    for k, v in ((5, 2003), (70, 2003), (5, 70001), (70, 70001)):
+        x = _logits(3, v, "fp32", gen)
+        ids, t, w, ls = _distill_inputs(x, k, gen, 0.5, lse, distinct=True)
+        t[1] = -INF
+        t[2, 1:] = -INF
+        out = B.vls_distill_loss(x, ids, t, w, ls, temperature=0.5)
+        _check_distill(x[::2], ids[::2], t[::2], w[::2], ls[::2] if lse else None,
+                       B.vls_distill_loss(*(a[::2].contiguous() if a is not None else None
+                                            for a in (x, ids, t, w, ls)), temperature=0.5), tau=0.5)
+        if lse:
+            assert out["row_loss"][1] == 0 and torch.count_nonzero(out["coef"][1]) == 0
+            assert torch.count_nonzero(out["dlogits"][1]) == 0
+        else:
+            assert torch.isnan(out["row_loss"][1]) and torch.isnan(out["coef"][1]).all()
+            assert torch.isnan(out["dlogits"][1]).all()

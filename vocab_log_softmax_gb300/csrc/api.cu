@@ -330,6 +330,7 @@ LossArgs loss_args(const void* x, int64_t N, int64_t V, vls_dtype dt, const int6
   a.vocab = V;
   a.cap = cap;
   a.inv_tau = 1.0f / temperature;
+  a.inv_tau_lo = static_cast<float>(1.0 / static_cast<double>(temperature) - static_cast<double>(a.inv_tau));
   a.ids = ids;
   a.k = k;
   a.ignore_index = ignore_index;

@@ -882,29 +882,35 @@ __device__ __forceinline__ void sweep_sync() { asm volatile("bar.sync 2, %0;" ::
 
 // What a distillation row needs beside the sums over the vocabulary, none of it
 // depending on them (so it overlaps the loads).  Each CTA of the row's cluster
-// takes the targets of its own columns: with t_j the teacher's logits over tau,
-// base and z0 the largest t_j and z_j among them, e_j = exp(t_j - base),
-//   P = sum e_j,   B = sum e_j ((t_j - base) - (z_j - z0) / tau).
-// With b the row's base (teacher_lse, or the largest of the CTAs'), f =
-// exp(base - b) and Z the sum of f P over the CTAs (1 with teacher_lse), the
-// teacher's probabilities are p_j = f e_j / Z and the row's loss is the sum over
-// CTAs of
-//   f / Z (B + P ((base - b) - log Z + (m - z0) / tau + log S)).
+// takes the targets of its own columns: with t_j the teacher's logits, base and
+// z0 the largest t_j and z_j among them, e_j = exp((t_j - base) / tau),
+//   P = sum e_j,   B = sum e_j ((t_j - base) - (z_j - z0)) / tau.
+// With b the largest base of the row's CTAs, s = b / tau - teacher_lse (0 without
+// it), f = exp((base - b) / tau + s) and Z the sum of f P over the CTAs (1 with
+// teacher_lse), the teacher's probabilities are p_j = f e_j / Z and the row's loss
+// is the sum over CTAs of
+//   f / Z (B + P ((base - b) / tau + s - log Z + (m - z0) / tau + log S)).
+// Logits are subtracted before they are scaled: a difference of two near ones is
+// exact, while t_j / tau is rounded at the size of t_j (at offset -8192 and tau =
+// 0.7 that alone moved p_j by 8e-4).  s, a difference of two large numbers, takes
+// 1 / tau in two floats.
 struct DistillPart {
-  float P, B, z0, base;
+  float P, B, z0, base;   // B times tau
 };
+// Three floats: with five, 16 bytes more of static shared memory, only 4 CTAs of
+// 43 KB and 64 targets fit an SM instead of 5 (4096 x 151936 bf16: 424 us, 405).
 struct DistillRow {
-  float b, inv, w;   // c_j = -w exp(t_j - b) inv
-  __device__ __forceinline__ float coef(float t) const { return -w * (ex2((t - b) * kLog2e) * inv); }
+  float b, shift, scale;   // c_j = scale 2^((t_j - b) kk + shift), kk = log2(e) / tau
+  __device__ __forceinline__ float weight(float t, float kk) const { return ex2(fmaf(t - b, kk, shift)); }
 };
 
 // One entry's share of P and B.
 template <bool CAP>
 __device__ __forceinline__ void part_add(float t, float x, float bc, float z0, const Scale& S, float& P, float& B) {
-  const float d = t - bc, e = ex2(d * kLog2e);
+  const float d = t - bc, e = ex2(d * S.kk);
   const float z = CAP ? cap_zr(x, S.K) : x;
   P += e;
-  if (e != 0.0f) B += e * (d - (z - z0) * S.inv_tau);
+  if (e != 0.0f) B += e * (d - (z - z0));
 }
 // Sums P and B over the warp (xor 16 exchanges one for the other, then 8..1)
 // and writes the part.
@@ -941,7 +947,7 @@ __device__ __forceinline__ int distill_few(const LossArgs& a, int64_t row, bool 
   for (int i = 0; i < 2; ++i) {
     const int j = lane + 32 * i;
     const int64_t id64 = j < k ? a.ids[at + j] : -1;
-    lt[i] = j < k ? load_teacher(a.teacher, a.teacher_dt, at + j) * S.inv_tau : 0.0f;
+    lt[i] = j < k ? load_teacher(a.teacher, a.teacher_dt, at + j) : 0.0f;
     const bool ok = valid_id(id64, a.vocab, a.ignore_index);
     if (first && !ok && j < k) a.coef[at + j] = 0.0f;
     id[i] = static_cast<int32_t>(id64);
@@ -982,7 +988,7 @@ static_assert(VLS_MAX_TOPK <= 4 * kLossThreads, "a thread takes up to 4 targets"
 constexpr int kTargetWords = VLS_MAX_TOPK / 32;
 template <class T>
 __device__ __forceinline__ void distill_collect(const LossArgs& a, int64_t row, bool first, const T* xr, int64_t col_beg,
-                                                int64_t col_end, const Targets& t, const Scale& S, uint32_t* masks) {
+                                                int64_t col_end, const Targets& t, uint32_t* masks) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t at = row * a.k;
   int32_t id[4];
@@ -994,7 +1000,7 @@ __device__ __forceinline__ void distill_collect(const LossArgs& a, int64_t row, 
     if (c * kLossThreads >= a.k) continue;
     const int j = c * kLossThreads + threadIdx.x;
     const int64_t id64 = j < a.k ? a.ids[at + j] : -1;
-    lt[c] = j < a.k ? load_teacher(a.teacher, a.teacher_dt, at + j) * S.inv_tau : 0.0f;
+    lt[c] = j < a.k ? load_teacher(a.teacher, a.teacher_dt, at + j) : 0.0f;
     const bool ok = valid_id(id64, a.vocab, a.ignore_index);
     if (first && !ok && j < a.k) a.coef[at + j] = 0.0f;
     id[c] = static_cast<int32_t>(id64);
@@ -1038,28 +1044,30 @@ __device__ __forceinline__ int distill_many(int k, const Targets& t, const Scale
 }
 
 // The row's loss, G and coefficients from its C CTAs' parts; warp 0.
-__device__ __forceinline__ float distill_finish(const DistillPart* parts, int C, float M, const LogSum& ls, float inv_tau,
-                                                bool known, float lse, float w, DistillRow* r, float* G) {
+__device__ __forceinline__ float distill_finish(const DistillPart* parts, int C, float M, const LogSum& ls, const Scale& S,
+                                                float inv_tau_lo, bool known, float lse, float w, DistillRow* r,
+                                                float* G) {
   const int lane = threadIdx.x & 31;
   const DistillPart d = lane < C ? parts[lane] : DistillPart{0.0f, 0.0f, 0.0f, neg_inf()};
-  const float b = known ? lse : warp_all<true>(d.base);
+  const float top = warp_all<true>(d.base), b = centre(top), base = centre(d.base);
+  const float shift = known ? fmaf(b, S.inv_tau, -lse) + b * inv_tau_lo : 0.0f;
+  *r = DistillRow{b, shift * kLog2e, 0.0f};
   // a CTA without targets, or all of whose e_j are 0, takes no part
-  const float gap = centre(d.base) - b;
-  const float f = d.P == 0.0f && b != neg_inf() ? 0.0f : ex2(gap * kLog2e);
+  const float f = d.P == 0.0f ? 0.0f : r->weight(base, S.kk);
   float Z = 1.0f, P = f * d.P;
 #pragma unroll
   for (int off = kLossMaxCluster / 2; off > 0; off >>= 1) P += __shfl_xor_sync(0xffffffffu, P, off);
   if (!known) Z = P;
   const float inv = 1.0f / Z;
+  r->scale = -w * inv;
   // log S - log Z from their parts: two numbers of like size that nearly cancel
   const LogSum lz = known ? LogSum{0.0f, 0.0f} : log_sum(Z);
-  const float logs = fmaf(ls.e - lz.e, kLn2, ls.lf - lz.lf);
-  float L = f != 0.0f ? f * (d.B + d.P * (gap + ((M - d.z0) * inv_tau + logs))) : 0.0f;
+  const float logs = fmaf(ls.e - lz.e, kLn2, ls.lf - lz.lf) + shift;
+  float L = f != 0.0f ? f * fmaf(S.inv_tau, d.B, d.P * fmaf((base - b) + (M - d.z0), S.inv_tau, logs)) : 0.0f;
 #pragma unroll
   for (int off = kLossMaxCluster / 2; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-  *r = DistillRow{b, inv, w};
   *G = -w * (P * inv);
-  return b == neg_inf() ? qnan() : L * inv;
+  return (known ? lse : top) == neg_inf() ? qnan() : L * inv;
 }
 
 // Whether a row has a valid id; most often its first one says so.
@@ -1259,7 +1267,7 @@ __global__ void __launch_bounds__(row_threads<LOSS>(), (loss_min_blocks<T, LOSS,
       if (a.teacher_lse != nullptr) tok.ref = a.teacher_lse[row];
     }
     if constexpr (HELP && !few) {
-      distill_collect(a, row, q == 0, xr, col_beg, col_end, t, S, s_masks);
+      distill_collect(a, row, q == 0, xr, col_beg, col_end, t, s_masks);
       asm volatile("bar.arrive 3, %0;" ::"n"(kLossThreads + 32) : "memory");
     }
     if constexpr (!HELP) {
@@ -1310,8 +1318,8 @@ __global__ void __launch_bounds__(row_threads<LOSS>(), (loss_min_blocks<T, LOSS,
     float dl = 0.0f, G = 0.0f;
     DistillRow dist;
     if constexpr (HELP)
-      dl = distill_finish(C > 1 ? dist_part : &s_part, C, st.m, ls, S.inv_tau, a.teacher_lse != nullptr, tok.ref,
-                          tok.w, &dist, &G);
+      dl = distill_finish(C > 1 ? dist_part : &s_part, C, st.m, ls, S, a.inv_tau_lo,
+                          a.teacher_lse != nullptr, tok.ref, tok.w, &dist, &G);
     if (lane == 0) {
       s_grad = finish_row<LOSS, CAP>(a, row, q == 0, st, ls, xt, tok, dl, G, S);
       if (HELP) s_dist = dist;
@@ -1323,7 +1331,7 @@ __global__ void __launch_bounds__(row_threads<LOSS>(), (loss_min_blocks<T, LOSS,
   const GradRow gr = s_grad;
   if constexpr (HELP) {
     for (int i = threadIdx.x; i < s_n; i += kLossThreads) {
-      const float c = s_dist.coef(t.g[i]);
+      const float c = s_dist.scale * s_dist.weight(t.g[i], S.kk);
       t.g[i] = c;
       a.coef[row * a.k + t.j[i]] = c;
     }

@@ -220,6 +220,7 @@ struct LossArgs {
   int64_t vocab;
   float cap;            // 0 = no softcap
   float inv_tau;        // 1 / temperature
+  float inv_tau_lo;     // and what its rounding left out
   const int64_t* ids;   // [N, k]
   int32_t k;
   int64_t ignore_index;
