@@ -412,7 +412,8 @@ typedef struct { float clip_low, clip_high, dual_clip, kl_coef; } vls_policy_cfg
  *   kl = exp(ref_logp - logp) - (ref_logp - logp) - 1,
  *   row_loss = -s + kl_coef kl;   loss = sum_r weights[r] row_loss[r].
  * The gradient passes where the unclipped term is the smaller one or r lies
- * inside the clip range, its ends included.  ids: int64 [N]; old_logp,
+ * inside the clip range, its ends included.  A NaN old_logp or advantage makes
+ * the token's row_loss, coef and gradient row NaN.  ids: int64 [N]; old_logp,
  * advantages, ref_logp (NULL: no KL term, kl_coef must be 0), weights: fp32
  * [N]; logp, row_loss, coef: fp32 [N]. */
 int vls_policy_loss(const void* logits, const vls_rows* rows, vls_dtype dt, int64_t N, int64_t V,

@@ -102,3 +102,41 @@ def test_teacher_rows_without_mass(lse):
         else:
             assert torch.isnan(out["row_loss"][1]) and torch.isnan(out["coef"][1]).all()
             assert torch.isnan(out["dlogits"][1]).all()
+
+
+# ---------------------------------------------------------------------------
+# NaN among a loss's constants
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("kl", [False, True])
+@pytest.mark.parametrize("dual", [0.0, 3.0])
+def test_policy_nan_constants(dtype, kl, dual):
+    """A NaN old_logp or advantage makes the token's loss NaN; its coefficient
+    and gradient row are NaN with it, wherever the ratio lies, and the other
+    rows keep their bits.  At an ignored id the constants are not looked at."""
+    gen = _gen(19)
+    n, v = 10, 1031
+    x = _logits(n, v, dtype, gen)
+    ids, old, adv, w, rf = _policy_inputs(x, gen, ignore=False)
+    rf = rf if kl else None
+    kw = dict(clip_low=0.2, clip_high=0.3, dual_clip=dual, kl_coef=0.05 if kl else 0.0)
+    ids[9] = -100
+    base = B.vls_policy_loss(x, ids, old, adv, w, rf, **kw)
+    logp = base["logp"]
+    old, adv = old.clone(), adv.clone()
+    old[0] = NAN
+    for i, step in ((1, 0.0), (2, 2.0), (3, -2.0), (4, 0.1)):     # ratios inside, above and below the clip range
+        old[i] = logp[i] - step
+        adv[i] = NAN
+    old[9] = adv[9] = NAN
+    out = B.vls_policy_loss(x, ids, old, adv, w, rf, **kw)
+    for i in range(5):
+        assert torch.isnan(out["row_loss"][i]) and torch.isnan(out["coef"][i]), i
+        assert torch.isnan(out["dlogits"][i]).all(), i
+    assert torch.isnan(out["loss"])
+    for key in ("row_loss", "logp", "coef", "dlogits"):
+        assert bitwise_equal(out[key][5:], base[key][5:]), key
+    again = B.vls_loss_bwd(x, ids, out["coef"], out["stats"])
+    assert torch.isnan(again[:5]).all() and bitwise_equal(again[5:], out["dlogits"][5:])

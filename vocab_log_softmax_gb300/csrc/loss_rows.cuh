@@ -842,7 +842,7 @@ __device__ __forceinline__ void grad_targets(T* dr, const Targets& t, int n, con
 //   L = pg + beta kl,
 // and dL/dlogp.  A token whose clipped term is the smaller one has no pg
 // gradient; at a border both terms agree and the gradient passes.  Comparisons
-// are written so that a NaN stays NaN.
+// are written so that a NaN ratio or advantage makes the loss and the gradient NaN.
 struct Token {
   float old, adv, ref, w;
 };
@@ -853,7 +853,7 @@ __device__ __forceinline__ float policy_token(float logp, const Token& t, float 
   const float rc = r < lo ? lo : (r > hi ? hi : r);
   const float s1 = r * adv, s2 = rc * adv;
   float gain = s2 < s1 ? s2 : s1;
-  float d = (rc == r || s1 < s2) ? -s1 : 0.0f;
+  float d = (rc == r || !(s1 >= s2)) ? -s1 : 0.0f;
   if (dual > 0.0f && adv < 0.0f) {
     const float least = dual * adv;
     if (gain <= least) {
