@@ -140,3 +140,64 @@ def test_policy_nan_constants(dtype, kl, dual):
         assert bitwise_equal(out[key][5:], base[key][5:]), key
     again = B.vls_loss_bwd(x, ids, out["coef"], out["stats"])
     assert torch.isnan(again[:5]).all() and bitwise_equal(again[5:], out["dlogits"][5:])
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "squared"])
+@pytest.mark.parametrize("where", ["margin", "ref", "logits"])
+def test_preference_nan(kind, where):
+    """A NaN in a pair makes its loss NaN and the gradient of every valid row of
+    the pair; the other pair keeps its bits."""
+    gen = _gen(23)
+    lengths = [4, 3, 5, 2]          # pairs (0, 2), (1, 3)
+    x = _logits(sum(lengths), 1031, "fp32", gen)
+    ids, offsets, rf, w, margin = _preference_inputs(x, lengths, gen)
+    ids[1] = -100
+    kw = dict(kind=kind, beta=0.5)
+    base = B.vls_preference_loss(x, ids, offsets, rf, w, margin, **kw)
+    x, rf, margin = x.clone(), rf.clone(), margin.clone()
+    if where == "margin":
+        margin[0] = NAN
+    elif where == "ref":
+        rf[2] = NAN
+    else:
+        x[2, 7] = NAN
+    out = B.vls_preference_loss(x, ids, offsets, rf, w, margin, **kw)
+    first = [0, 2, 3] + list(range(7, 12))
+    second = list(range(4, 7)) + [12, 13]
+    assert torch.isnan(out["pair_loss"][0]) and torch.isnan(out["coef"][first]).all()
+    assert torch.isnan(out["dlogits"][first]).all()
+    assert torch.count_nonzero(out["dlogits"][1]) == 0 and out["coef"][1] == 0
+    for key in ("logp", "coef", "dlogits"):
+        assert bitwise_equal(out[key][second], base[key][second]), key
+    assert bitwise_equal(out["pair_loss"][1:], base["pair_loss"][1:])
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "squared"])
+def test_preference_infinities(kind):
+    """A target of probability 0, masked columns and columns of the type's lowest
+    value: the rewards are infinite where the definition's are, u is infinite on
+    the right and on the wrong side, and no finite row has a NaN."""
+    gen = _gen(24)
+    lengths = [3, 3, 3, 3, 3, 3]     # pairs (0, 3), (1, 4), (2, 5)
+    x = _logits(18, 1031, "bf16", gen)
+    ids, offsets, rf, w, _ = _preference_inputs(x, lengths, gen)
+    x[0, : 1031 // 2] = torch.finfo(torch.bfloat16).min
+    ids[0] = 1030
+    x[4, ::3] = -INF
+    ids[4] = 1
+    rf[0] = rf[4] = -5.0
+    x[7, ids[7]] = -INF              # pair 2: the preferred one has probability 0
+    x[12, ids[12]] = -INF            # pair 1: the other one has
+    out = B.vls_preference_loss(x, ids, offsets, rf, w, kind=kind, beta=0.5)
+    with np.errstate(all="ignore"):
+        r = ref.preference(to_f64(x), _np(ids), _np(offsets), _np(rf), None, _np(w), kind, 0.5)
+    for key in ("logp", "pair_loss", "reward"):
+        got, want = _np(out[key]), r[key]
+        assert np.array_equal(np.isinf(got), np.isinf(want)) and not np.isnan(got).any(), key
+        assert np.array_equal(got[np.isinf(got)], want[np.isinf(want)]), key
+    fine = np.isfinite(r["coef"])
+    assert np.array_equal(np.isfinite(_np(out["coef"])), fine)
+    g = ref.grad_rows(to_f64(x), _np(ids)[:, None], _np(out["coef"])[:, None])
+    assert_grad_close(out["dlogits"][torch.tensor(fine)], g[fine], "dlogits")

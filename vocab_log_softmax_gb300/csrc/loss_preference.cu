@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
       if (isnan(u)) loss = u;
     } else if (a.kind == VLS_PREF_HINGE) {
       loss = u < 1.0f ? 1.0f - u : (isnan(u) ? u : 0.0f);
-      du = u < 1.0f ? -1.0f : 0.0f;
+      du = u < 1.0f ? -1.0f : (isnan(u) ? u : 0.0f);
     } else {
       const float e = (u - 0.5f) / beta;   // (u / beta - 1 / (2 beta))^2
       loss = e * e;
