@@ -201,3 +201,20 @@ def test_preference_infinities(kind):
     assert np.array_equal(np.isfinite(_np(out["coef"])), fine)
     g = ref.grad_rows(to_f64(x), _np(ids)[:, None], _np(out["coef"])[:, None])
     assert_grad_close(out["dlogits"][torch.tensor(fine)], g[fine], "dlogits")
+
+
+@gpu
+def test_policy_zero_advantage_beyond_fp32():
+    """A ratio that overflows fp32 (log-probability 100 above the recorded one)
+    times an advantage of 0 is 0, as in the definition; with a recorded
+    probability of 0 the ratio is infinite and 0 times it is NaN."""
+    x = torch.zeros((4, 2), device=DEV)
+    ids = torch.zeros(4, dtype=torch.int64, device=DEV)
+    old = torch.tensor([-100.0, -100.0, -INF, -100.0], device=DEV)
+    adv = torch.tensor([0.0, -0.0, 0.0, 1.0], device=DEV)
+    for dual in (0.0, 3.0):
+        out = B.vls_policy_loss(x, ids, old, adv, None, None, dual_clip=dual)
+        assert out["row_loss"][:2].tolist() == [0.0, 0.0] and out["coef"][:2].tolist() == [0.0, 0.0]
+        assert torch.count_nonzero(out["dlogits"][:2]) == 0
+        assert torch.isnan(out["row_loss"][2]) and torch.isnan(out["coef"][2])
+        assert abs(out["row_loss"][3].item() + 1.2) < 1e-6 and out["coef"][3] == 0

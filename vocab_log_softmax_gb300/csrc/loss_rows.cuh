@@ -851,7 +851,8 @@ __device__ __forceinline__ float policy_token(float logp, const Token& t, float 
   const float adv = t.adv;
   const float r = expf(logp - t.old);
   const float rc = r < lo ? lo : (r > hi ? hi : r);
-  const float s1 = r * adv, s2 = rc * adv;
+  // a ratio beyond fp32 (log r > 88) of a finite old_logp times 0 is 0
+  const float s1 = adv == 0.0f && r == pos_inf() && t.old > neg_inf() ? 0.0f : r * adv, s2 = rc * adv;
   float gain = s2 < s1 ? s2 : s1;
   float d = (rc == r || !(s1 >= s2)) ? -s1 : 0.0f;
   if (dual > 0.0f && adv < 0.0f) {
