@@ -450,7 +450,8 @@ typedef struct { int32_t kind; int32_t length_average; float beta; float label_s
 
 /* Paired log ratios.  The N rows hold 2 P sequences one after the other:
  * sequence s is rows offsets[s] to offsets[s + 1] - 1 (int64 [2 P + 1], on the
- * device, ascending, at most N; rows outside every sequence take no part).
+ * device, ascending, at most N; rows outside every sequence take no part: their
+ * coef and stats are 0 and their gradient rows exactly 0, whatever the logits).
  * Sequence i < P is preferred over sequence P + i:
  *   R_s = sum over its rows with a valid id of (log q[id] - ref_logp),
  *   u_i = beta (R_i - R_{P+i}) - margin[i],   reward_s = beta R_s,

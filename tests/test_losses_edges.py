@@ -218,3 +218,60 @@ def test_policy_zero_advantage_beyond_fp32():
         assert torch.count_nonzero(out["dlogits"][:2]) == 0
         assert torch.isnan(out["row_loss"][2]) and torch.isnan(out["coef"][2])
         assert abs(out["row_loss"][3].item() + 1.2) < 1e-6 and out["coef"][3] == 0
+
+
+# ---------------------------------------------------------------------------
+# preference: rows outside every sequence
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("v", [1031, 70000])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_rows_outside_every_sequence(dtype, v, cap):
+    """The rows before the first sequence and behind the last take no part
+    whatever they hold (a buffer's unused end): valid ids on logits that are NaN,
+    infinite or all -inf get a gradient of exactly 0, from the call and from its
+    statistics."""
+    gen = _gen(25)
+    lengths = [4, 3]
+    x = _logits(2 + sum(lengths) + 5, v, dtype, gen)
+    ids, offsets, rf, w, margin = _preference_inputs(x, lengths, gen, lead=2, cap=cap)
+    base = B.vls_preference_loss(x, ids, offsets, rf, w, margin, cap=cap)
+    x = x.clone()
+    x[0] = NAN
+    x[1, 3] = INF
+    x[9] = -INF
+    x[10, 0] = NAN
+    x[11] = INF
+    x[12, 1:] = -INF
+    out = B.vls_preference_loss(x, ids, offsets, rf, w, margin, cap=cap)
+    inside, outside = slice(2, 9), [0, 1] + list(range(9, 14))
+    for key in ("loss", "pair_loss", "reward"):
+        assert bitwise_equal(out[key].reshape(-1), base[key].reshape(-1)), key
+    for key in ("logp", "coef", "dlogits"):
+        assert bitwise_equal(out[key][inside], base[key][inside]), key
+    assert torch.equal(out["coef"][outside], torch.zeros(7, device=DEV))
+    assert torch.equal(out["dlogits"][outside], torch.zeros_like(out["dlogits"][outside]))
+    for up in (1.0, -0.37):
+        again = B.vls_loss_bwd(x, ids, out["coef"], out["stats"], torch.tensor(up, device=DEV), cap=cap)
+        assert torch.equal(again[outside], torch.zeros_like(again[outside]))
+        assert torch.isfinite(again[inside]).all()
+    leaf = x.clone().requires_grad_(True)
+    (3.0 * vls.preference_loss(leaf, ids, offsets, ref_logp=rf, softcap=cap or None)[0]).backward()
+    assert torch.equal(leaf.grad[outside], torch.zeros_like(leaf.grad[outside]))
+
+
+@gpu
+def test_one_column_rows_keep_their_gradient():
+    """Rows whose statistics are those of a row without a target (max 0, log-sum
+    0): one column, or one column that holds all the mass."""
+    x = torch.tensor([[0.0, -200.0], [0.0, -200.0], [0.0, -200.0]], device=DEV)
+    ids = torch.tensor([0, 1, 1], device=DEV)
+    offsets = torch.tensor([0, 1, 3], device=DEV)
+    for kind in ("sigmoid", "squared"):     # u = 100: the coefficients are 2e-44 and 398
+        out = B.vls_preference_loss(x, ids, offsets, torch.full((3,), -200.0, device=DEV), kind=kind, beta=0.5)
+        assert _np(out["stats"]).tolist() == [[0.0, 0.0]] * 3
+        g = ref.grad_rows(to_f64(x), _np(ids)[:, None], _np(out["coef"])[:, None])
+        assert_grad_close(out["dlogits"], g)
+    assert torch.count_nonzero(out["coef"]) == 3 and torch.count_nonzero(out["dlogits"][1:]) == 4

@@ -1162,6 +1162,7 @@ int vls_preference_loss(const void* logits, const vls_rows* rows, vls_dtype dt, 
   p.pair_loss = pair_loss;
   p.reward = reward;
   p.coef = coef;
+  p.stats = stats;
   if (int e = VLS_LAUNCH(launch_loss_pairs(p, N > 0, s))) return e;
   if (N == 0 || !dlogits) return VLS_LAUNCH(launch_loss_sum(pair_loss, weights, P, loss, s));
   g.sum_v = pair_loss;

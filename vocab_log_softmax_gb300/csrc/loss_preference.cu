@@ -29,7 +29,9 @@ __device__ __forceinline__ int block_count(int n) {
 // (logp - ref), in two floats because a long answer's sum is hundreds of times
 // the difference that matters; u = beta (R_chosen - R_rejected) - margin, its loss
 // and the coefficient dL/dlogp of every row of the two sequences.  The last
-// CTA writes the coefficient 0 of the rows that no sequence holds.  Bound by
+// CTA gives the rows that no sequence holds the coefficient and statistics of a
+// row without a target, so that whatever their logits hold reaches no gradient.
+// Bound by
 // latency (two dependent sweeps of 20 bytes a row): a few us beside the launches
 // over the logits, hidden in part by the dependent launch (3 launches over 64 x
 // 32000 bf16 in 10.5 us).
@@ -42,8 +44,12 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   auto clip_row = [&](int64_t r) { return r < 0 ? 0 : (r > a.rows ? a.rows : r); };
   if (blockIdx.x == P) {
     const int64_t first = clip_row(a.offsets[0]), last = clip_row(a.offsets[2 * P]);
-    for (int64_t r = threadIdx.x; r < first; r += kPairThreads) a.coef[r] = 0.0f;
-    for (int64_t r = last + threadIdx.x; r < a.rows; r += kPairThreads) a.coef[r] = 0.0f;
+    auto clear = [&](int64_t r) {
+      a.coef[r] = 0.0f;
+      a.stats[r] = vls_rowstat{0.0f, 0.0f};
+    };
+    for (int64_t r = threadIdx.x; r < first; r += kPairThreads) clear(r);
+    for (int64_t r = last + threadIdx.x; r < a.rows; r += kPairThreads) clear(r);
     return;
   }
   const int64_t pair = blockIdx.x;

@@ -1458,7 +1458,14 @@ __global__ void __launch_bounds__(kLossThreads, 5) loss_grad_kernel(const LossGr
   if constexpr (!TOPK) {
     id = a.ids[row];
     any = valid_id(id, V, a.ignore_index);
-    if (any) gr.G = a.coef[row] * up;
+    if (any) {
+      const float c = a.coef[row];
+      // A row that takes no part in its loss has statistics 0.  A row's own may be
+      // 0 as well, but then its logits are finite or -inf, and a coefficient of 0
+      // makes its gradient 0 all the same.
+      any = c != 0.0f || st.m != 0.0f || st.log_s != 0.0f;
+      gr.G = c * up;
+    }
   } else {
     targets_load(t, threadIdx.x, kLossThreads, a.ids + row * a.k, a.k, V, a.ignore_index,
                  [&](int j, bool ok) { return ok ? a.coef[row * a.k + j] : 0.0f; });

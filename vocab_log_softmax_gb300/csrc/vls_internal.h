@@ -290,6 +290,7 @@ struct PairArgs {
   float* pair_loss;     // [P]
   float* reward;        // [2 P]
   float* coef;          // [N]
+  vls_rowstat* stats;   // [N]; written for the rows that no sequence holds
 };
 
 // Launchers: one per kernel family, dispatching on dtype and softcap.  They
