@@ -275,3 +275,35 @@ def test_one_column_rows_keep_their_gradient():
         g = ref.grad_rows(to_f64(x), _np(ids)[:, None], _np(out["coef"])[:, None])
         assert_grad_close(out["dlogits"], g)
     assert torch.count_nonzero(out["coef"]) == 3 and torch.count_nonzero(out["dlogits"][1:]) == 4
+
+
+# ---------------------------------------------------------------------------
+# shapes of the constants, temperatures
+# ---------------------------------------------------------------------------
+
+def test_constants_of_another_shape():
+    """[T, B] constants beside [B, T, V] logits would be taken in the wrong
+    order.  The leading dimensions' shape, one flattened dimension and shapes that
+    differ by dimensions of size 1 say the same order."""
+    b, t, v = 2, 3, 6
+    x, i = torch.zeros((b, t, v)), torch.zeros((b, t), dtype=torch.int64)
+    f, wrong = torch.zeros((b, t)), torch.zeros((t, b))
+    for kw in (dict(old_logp=wrong, advantages=f), dict(old_logp=f, advantages=wrong),
+               dict(old_logp=f, advantages=f, ref_logp=wrong), dict(old_logp=f, advantages=f, weights=wrong)):
+        with pytest.raises(ValueError, match="shape"):
+            vls.policy_loss(x, i, **kw)
+    for kw in (dict(teacher_lse=wrong), dict(weights=wrong)):
+        with pytest.raises(ValueError, match="shape"):
+            vls.distill_loss(x, i[..., None], f[..., None], **kw)
+    y, j, g = torch.zeros((6, 2, v)), torch.zeros((6, 2), dtype=torch.int64), torch.zeros((2, 6))
+    with pytest.raises(ValueError, match="shape"):
+        vls.preference_loss(y, j, ref_logp=g)
+    values = torch.arange(6.0)
+    for shape in ((2, 3), (6,), (2, 3, 1), (1, 2, 3), (2, 1, 3)):
+        assert vls._const(values.view(shape), torch.Size((2, 3)), "a").tolist() == values.tolist()
+    assert vls._const(values.view(2, 3), values.shape, "a").tolist() == values.tolist()    # flattened logits
+    assert vls._const(torch.ones(()), torch.Size(()), "a").tolist() == [1.0]
+    assert vls._const(None, torch.Size((2, 3)), "a") is None
+    for shape in ((3, 2), (5,), (1, 6, 2)):
+        with pytest.raises(ValueError):
+            vls._const(torch.zeros(shape), torch.Size((2, 3)), "a")

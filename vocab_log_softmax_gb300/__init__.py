@@ -293,12 +293,15 @@ def linear_logprobs(hidden: torch.Tensor, weight: torch.Tensor, ids: torch.Tenso
 # training losses
 # ---------------------------------------------------------------------------
 
-def _const(t, n: int, what: str):
-    """A constant input of a loss: [n] float32 contiguous, detached (None stays None)."""
+def _const(t, shape, what: str):
+    """A constant input of a loss, of the given shape: float32, contiguous,
+    flattened and detached (None stays None).  Dimensions of size 1 and one
+    flattened dimension leave no doubt about the order; other shapes are refused."""
     if t is None:
         return None
-    if t.numel() != n:
-        raise ValueError(f"{what} must have {n} elements, not {t.numel()}")
+    have, want = ([d for d in s if d != 1] for s in (t.shape, shape))
+    if t.numel() != shape.numel() or (have != want and min(len(have), len(want)) > 1):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     return t.detach().reshape(-1).to(torch.float32).contiguous()
 
 
@@ -369,8 +372,9 @@ def policy_loss(logits: torch.Tensor, ids: torch.Tensor, old_logp: torch.Tensor,
     n, lead = logits.shape[:-1].numel(), logits.shape[:-1]
     ids2 = _loss_ids(ids, logits, n, None)
     cap = _cap(softcap)
-    w = _const(weights, n, "weights") if weights is not None else _mean_weights(ids2, logits.shape[-1], ignore_index)
-    old, adv, ref = _const(old_logp, n, "old_logp"), _const(advantages, n, "advantages"), _const(ref_logp, n, "ref_logp")
+    w = _const(weights, lead, "weights") if weights is not None else _mean_weights(ids2, logits.shape[-1], ignore_index)
+    old, adv = _const(old_logp, lead, "old_logp"), _const(advantages, lead, "advantages")
+    ref = _const(ref_logp, lead, "ref_logp")
 
     def call(rows, grad):
         return vls_policy_loss(rows, ids2, old, adv, w, ref, clip_low=clip_low, clip_high=clip_high,
@@ -405,8 +409,8 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher_logits: torch.
         raise ValueError(f"teacher_logits must have the ids' shape {tuple(ids.shape)}, not {tuple(teacher_logits.shape)}")
     teacher = teacher_logits.detach().contiguous()
     cap = _cap(softcap)
-    w = _const(weights, n, "weights") if weights is not None else _mean_weights(ids2, logits.shape[-1], ignore_index)
-    lse = _const(teacher_lse, n, "teacher_lse")
+    w = _const(weights, lead, "weights") if weights is not None else _mean_weights(ids2, logits.shape[-1], ignore_index)
+    lse = _const(teacher_lse, lead, "teacher_lse")
 
     def call(rows, grad):
         return vls_distill_loss(rows, ids2, teacher, w, lse, ignore_index=int(ignore_index), cap=cap,
@@ -448,9 +452,10 @@ def preference_loss(logits: torch.Tensor, ids: torch.Tensor, offsets: torch.Tens
     if pairs < 1 or offsets.numel() != 2 * pairs + 1:
         raise ValueError("offsets must have 2P + 1 elements, P >= 1")
     cap = _cap(softcap)
-    w = (_const(weights, pairs, "weights") if weights is not None
+    per_pair = torch.Size((pairs,))
+    w = (_const(weights, per_pair, "weights") if weights is not None
          else torch.full((pairs,), 1.0 / pairs, dtype=torch.float32, device=logits.device))
-    ref, mar = _const(ref_logp, n, "ref_logp"), _const(margin, pairs, "margin")
+    ref, mar = _const(ref_logp, lead, "ref_logp"), _const(margin, per_pair, "margin")
 
     def call(rows, grad):
         return vls_preference_loss(rows, ids2, offsets, ref, w, mar, kind=kind, beta=beta,
