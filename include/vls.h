@@ -395,7 +395,8 @@ int vls_linear_logp_fwd_noalloc(const void* h, int64_t ldh, const void* W, int64
 /*    read: its terms, coef and stats are 0 and its gradient row exactly 0.   */
 /*    A row with a valid id whose logits are all -inf, or hold a NaN, has NaN */
 /*    terms and a NaN gradient row.                                          */
-/*  - temperature is finite and > 0.  V < 2^31.                               */
+/*  - temperature is finite and > 0, large enough that 1.5 / temperature and,  */
+/*    with a cap, 2.9 cap / temperature are fp32 numbers.  V < 2^31.          */
 /*  - N == 0 returns VLS_OK and writes nothing (the preference call: only     */
 /*    with P == 0).                                                          */
 /* ------------------------------------------------------------------------ */

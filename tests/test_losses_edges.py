@@ -307,3 +307,25 @@ def test_constants_of_another_shape():
     for shape in ((3, 2), (5,), (1, 6, 2)):
         with pytest.raises(ValueError):
             vls._const(torch.zeros(shape), torch.Size((2, 3)), "a")
+
+
+def test_temperatures_whose_exponents_overflow():
+    """log2(e) / temperature, and 2 cap log2(e) / temperature with a softcap, have
+    to be fp32 numbers; smaller temperatures are refused by every call."""
+    build.build()
+    tlib = _lib.load_test()
+    assert tlib.vls_test_set_fault(_lib.VLS_TEST_FAULT_DEVICE) == 0
+    rows = _lib.rows(10)
+
+    def calls(cap, tau):
+        cfg = _lib.VlsPolicyCfg(0.2, 0.2, 0.0, 0.0)
+        yield tlib.vls_policy_loss(P, rows, 1, 4, 10, P, -100, cap, tau, cfg, P, P, None, None, P, P, P, P, P, P, None)
+        yield tlib.vls_distill_loss(P, rows, 1, 4, 10, P, 3, -100, cap, tau, P, 0, None, None, P, P, P, P, P, None)
+        yield tlib.vls_loss_bwd(P, rows, 1, 4, 10, P, 1, -100, cap, tau, P, P, None, 0, P, None)
+
+    try:
+        for cap, tau, code in ((0.0, 3.5e-39, 7), (0.0, 4.5e-39, 5), (30.0, 2.0e-37, 7), (30.0, 3.0e-37, 5),
+                               (1e30, 1e-9, 7), (1e30, 1e-7, 5), (0.0, 1e-3, 5), (0.0, 3e38, 5), (30.0, 1.0, 5)):
+            assert list(calls(cap, tau)) == [code] * 3, (cap, tau)
+    finally:
+        tlib.vls_test_set_fault(_lib.VLS_TEST_FAULT_NONE)

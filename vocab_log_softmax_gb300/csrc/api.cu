@@ -310,7 +310,13 @@ void loss_geometry(int64_t V, vls_dtype dt, int* cluster, int64_t* vec_per_cta) 
   *cluster = static_cast<int>(ceil_div(nvec, *vec_per_cta));
 }
 
-int check_temperature(float t) { return (std::isfinite(t) && t > 0.0f && std::isfinite(1.0f / t)) ? VLS_OK : VLS_ERR_ARG; }
+// The kernels scale by log2(e) / t, and with a cap by 2 cap log2(e) / t: both have
+// to be fp32 numbers (infinity times a difference of 0 would be NaN).
+int check_temperature(float t, float cap) {
+  if (!(std::isfinite(t) && t > 0.0f && std::isfinite(1.0f / t))) return VLS_ERR_ARG;
+  const double scale = 1.4426950408889634 / static_cast<double>(t) * (cap > 0.5f ? 2.0 * static_cast<double>(cap) : 1.0);
+  return scale < 3.4e38 ? VLS_OK : VLS_ERR_ARG;
+}
 
 // The row checks shared by the loss calls, before any pointer is looked at.
 int check_loss(int64_t N, int64_t V, int32_t k, vls_dtype dt, float cap, float temperature) {
@@ -318,7 +324,7 @@ int check_loss(int64_t N, int64_t V, int32_t k, vls_dtype dt, float cap, float t
   if (V > kMaxGrid || k < 1 || k > VLS_MAX_TOPK) return VLS_ERR_SHAPE;
   if (!dtype_ok(dt)) return VLS_ERR_DTYPE;
   if (int e = check_row_cap(cap)) return e;
-  return check_temperature(temperature);
+  return check_temperature(temperature, cap);
 }
 
 LossArgs loss_args(const void* x, int64_t N, int64_t V, vls_dtype dt, const int64_t* ids, int32_t k,
