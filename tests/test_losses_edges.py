@@ -278,6 +278,81 @@ def test_one_column_rows_keep_their_gradient():
 
 
 # ---------------------------------------------------------------------------
+# distillation with more than 64 targets: kernels of their own
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("cap,tau", [(0.0, 1.0), (0.0, 2.0), (30.0, 1.0), (30.0, 0.5)])
+@pytest.mark.parametrize("lse", [False, True])
+@pytest.mark.parametrize("k,v", [(70, 30011), (300, 30011), (70, 151936), (1024, 151937)])
+def test_distill_forms_of_many_targets(dtype, cap, tau, lse, k, v):
+    gen = _gen(k + v)
+    x = _logits(3, v, dtype, gen, 5.0)
+    args = _distill_inputs(x, k, gen, tau, lse, distinct=True)
+    out = B.vls_distill_loss(x, *args, cap=cap, temperature=tau)
+    _check_distill(x, *args, out, cap, tau)
+
+
+@gpu
+@pytest.mark.parametrize("tdt", sorted(DTYPES))
+@pytest.mark.parametrize("lse", [False, True])
+@pytest.mark.parametrize("k,v", [(12, 70001), (65, 2003), (70, 70001), (513, 70000)])
+def test_many_targets_ragged_rows_and_masks(tdt, lse, k, v):
+    """As test_distill_ragged_rows_and_masks, on rows of one CTA and of several."""
+    gen = _gen(29)
+    n = 10
+    x = _logits(n, v, "bf16", gen)
+    ids, t, w, ls = _distill_inputs(x, k, gen, 1.0, lse)
+    t = t.to(DTYPES[tdt])
+    ids[0, 4:] = -100
+    ids[1, :] = -100
+    ids[2, :] = 77
+    ids[3, ::2] = v
+    t[4, :5] = -INF
+    x[5, ids[5, 0]] = -INF
+    ids[5, 1:] = torch.arange(1, k, device=DEV) + 5 + ids[5, 0] % 900
+    t[6, 0] = -INF
+    ids[6] = torch.arange(k, device=DEV) * 3
+    x[6, 0] = -INF
+    x[7, :] = -INF
+    x[8, 3] = NAN
+    x[9, :] = -INF
+    ids[9, :] = -1
+    out = B.vls_distill_loss(x, ids, t, w, ls)
+    r = _check_distill(x, ids, t, w, ls, out)
+    assert np.isposinf(r["row_loss"][5]) and np.isnan(r["row_loss"][7]) and np.isnan(r["row_loss"][8])
+    assert np.isfinite(r["row_loss"][6]) and r["row_loss"][1] == 0 and r["row_loss"][9] == 0
+    for i in (1, 9):
+        assert torch.count_nonzero(out["dlogits"][i]) == 0 and torch.count_nonzero(out["coef"][i]) == 0
+    g = B.vls_loss_bwd(x, ids, out["coef"], out["stats"])
+    fine = [0, 1, 2, 3, 4, 5, 6, 9]
+    assert_grad_close(g[fine], to_f64(out["dlogits"])[fine], "again")
+
+
+@gpu
+@pytest.mark.parametrize("k", [9, 70, 300])
+def test_many_targets_invariance(k):
+    """Bits do not depend on the layout, on the other rows, on a repetition or on
+    whether the gradient is asked for."""
+    gen = _gen(30)
+    x = _logits(20, 70003, "bf16", gen)
+    args = _distill_inputs(x, k, gen, 0.7, True)
+    kw = dict(temperature=0.7)
+    full = B.vls_distill_loss(x, *args, **kw)
+    wide = torch.full((20, 70003 + 13), 5.0, dtype=x.dtype, device=DEV)
+    wide[:, :70003] = x
+    quiet = B.vls_distill_loss(x, *args, grad=False, **kw)
+    for key in full:
+        assert bitwise_equal(full[key], B.vls_distill_loss(wide[:, :70003], *args, **kw)[key]), key
+        assert key == "dlogits" or bitwise_equal(full[key], quiet[key]), key
+    p = torch.tensor([19, 3, 11], device=DEV)
+    part = B.vls_distill_loss(x[p], *(a[p].contiguous() for a in args), **kw)
+    for key in ("row_loss", "coef", "stats", "dlogits"):
+        assert bitwise_equal(full[key][p], part[key]), key
+
+
+# ---------------------------------------------------------------------------
 # shapes of the constants, temperatures
 # ---------------------------------------------------------------------------
 
