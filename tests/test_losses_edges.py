@@ -352,6 +352,21 @@ def test_many_targets_invariance(k):
         assert bitwise_equal(full[key][p], part[key]), key
 
 
+@gpu
+@pytest.mark.parametrize("dtype,v", [("bf16", 1638400), ("bf16", 1638399), ("bf16", 1638401), ("fp32", 819200),
+                                     ("fp32", 819201)])
+def test_longest_staged_rows(dtype, v):
+    """Rows that fill the shared memory of the largest cluster, with the most
+    targets beside them, and rows one column longer."""
+    gen = _gen(v)
+    x = _logits(2, v, dtype, gen)
+    args = _policy_inputs(x, gen)
+    _check_policy(x, *args, B.vls_policy_loss(x, *args, **CFG), what="policy")
+    for k in (64, 1024):
+        d = _distill_inputs(x, k, gen)
+        _check_distill(x, *d, B.vls_distill_loss(x, *d), what=f"distill k={k}")
+
+
 # ---------------------------------------------------------------------------
 # shapes of the constants, temperatures
 # ---------------------------------------------------------------------------

@@ -409,7 +409,8 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher_logits: torch.
         raise ValueError(f"teacher_logits must have the ids' shape {tuple(ids.shape)}, not {tuple(teacher_logits.shape)}")
     teacher = teacher_logits.detach().contiguous()
     cap = _cap(softcap)
-    w = _const(weights, lead, "weights") if weights is not None else _mean_weights(ids2, logits.shape[-1], ignore_index)
+    w = (_const(weights, lead, "weights") if weights is not None
+         else _mean_weights(ids2, logits.shape[-1], ignore_index))
     lse = _const(teacher_lse, lead, "teacher_lse")
 
     def call(rows, grad):

@@ -654,8 +654,9 @@ def vls_preference_loss(logits: torch.Tensor, ids: torch.Tensor, offsets: torch.
     d = _grad_out(dlogits, grad, n, v, logits)
     loss, pair_loss, reward, logp, coef, stats = _loss_out(dev, pairs > 0, (), pairs, 2 * pairs, n, n, (n, 2))
     st = lib.vls_preference_loss(logits.data_ptr(), lay, dt, n, v, ids.data_ptr(), ignore_index, cap, offsets.data_ptr(),
-                                 pairs, cfg, p_ref, p_mar, p_w, loss.data_ptr(), pair_loss.data_ptr(), reward.data_ptr(),
-                                 logp.data_ptr(), coef.data_ptr(), stats.data_ptr(), _ptr(d), _raw_stream(dev, stream))
+                                 pairs, cfg, p_ref, p_mar, p_w, loss.data_ptr(), pair_loss.data_ptr(),
+                                 reward.data_ptr(), logp.data_ptr(), coef.data_ptr(), stats.data_ptr(), _ptr(d),
+                                 _raw_stream(dev, stream))
     _lib.check("vls_preference_loss", st)
     return {"loss": loss, "pair_loss": pair_loss, "reward": reward, "logp": logp, "coef": coef, "stats": stats,
             "dlogits": d}

@@ -291,12 +291,12 @@ int check_shard(int64_t N, int64_t V_shard, int64_t offset, int64_t V_total) {
 // Cluster of the loss rows: a function of V and the dtype only.  A row is cut
 // into the fewest runs of at most kLossRun16 or kLossRun32 bytes, so that 5
 // (16-bit) or 4 (fp32, by registers) CTAs with their runs share an SM and their
-// load, wait and store phases interleave.  Measured (with two passes over the
-// staged run, now one), us: 4096 x 151936 bf16 policy 397 at 43 KB runs (7 CTAs a
-// row, 5 an SM), 412 at 38 KB, 403 at 51 KB (4 an SM); softcapped 2048 x 262144 555 at 44 KB, 634 at 37 KB, 599 at 48 KB; 2048 x
-// 151936 fp32 policy 382 at 51 KB, 471 at 43 KB, 398 at 61 KB.  A 16-bit row of up
-// to 64 KB stays whole: 18750 x 32000 bf16 policy 361 us, 394 in two runs.  Above 8
-// CTAs a row: 1024 x 262144 fp32 policy 432 against 603 with 8.
+// load, wait and store phases interleave.  us: 4096 x 151936 bf16 policy 386 at 43
+// KB runs (7 CTAs a row, 5 an SM), 405 at 38 KB, 397 at 51 KB (4 an SM); softcapped
+// 2048 x 262144 547 at 44 KB, 624 at 37 KB, 586 at 51 KB; 2048 x 151936 fp32 policy
+// 384 at 51 KB, 442 at 43 KB, 394 at 61 KB.  A 16-bit row of up to 64 KB stays whole:
+// 18750 x 32000 bf16 policy 363 us, 397 in two runs.  Above 8 CTAs a row: 1024 x
+// 262144 fp32 policy 406 against 608 with 8.
 constexpr int64_t kLossRun16 = 44000, kLossRun32 = 52500;
 // Longest run that is held in shared memory: the CTA's limit less what 1024
 // targets and the granules around the run take.

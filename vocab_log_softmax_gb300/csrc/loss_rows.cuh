@@ -197,8 +197,7 @@ struct RowSum {
 // --------------------------------------------------------------------------
 // A row's run in shared memory.  The copy keeps the run's phase within a
 // 16-byte granule, so that all but the ends move in whole granules whatever
-// the row's alignment; a vector of 8 columns is then read from one or two
-// (fp32: two or three) granules.
+// the row's alignment; a unit of columns is then read from one or two granules.
 // --------------------------------------------------------------------------
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -210,7 +209,7 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   return r;
 }
 
-// 8 elements that start `shift` elements (uniform over the CTA) behind a
+// A unit of columns that starts `shift` elements (uniform over the CTA) behind a
 // granule boundary, from the granules there: whole words by SW, known to the
 // compiler (with_shift), and for 16-bit types a last half word by a funnel
 // shift of `bits`.
@@ -347,12 +346,11 @@ struct Stage {
   __device__ __forceinline__ void start(const T* run, unsigned char* smem) const {
     T* own = reinterpret_cast<T*>(smem + 16) + phase;
     if (ALIGNED || phase == 0) {
+      static_assert(kCols<T> == kPer, "a unit is a granule");
       const int nvec = (cols + kCols<T> - 1) / kCols<T>;
       for (int v = threadIdx.x; v < nvec; v += kLossThreads) {
         if (kCols<T> * v + kCols<T> <= cols) {
-#pragma unroll
-          for (int h = 0; h < kCols<T> / kPer; ++h)
-            cp_async16(base + static_cast<uint32_t>(kCols<T> * v + h * kPer) * sizeof(T), run + kCols<T> * v + h * kPer);
+          cp_async16(base + 16u * static_cast<uint32_t>(v), run + kCols<T> * v);
         } else {
           for (int c = kCols<T> * v; c < cols; ++c) own[c] = run[c];
         }
@@ -368,7 +366,7 @@ struct Stage {
       if (static_cast<int>(threadIdx.x) < cols - tail) own[tail + threadIdx.x] = run[tail + threadIdx.x];
     }
   }
-  // the 8 elements from element e on, e + phase a multiple of a granule
+  // the unit from element e on, e + phase a multiple of a granule
   __device__ __forceinline__ void aligned(Unit<T>& r, int e) const {
     const uint32_t g = base + static_cast<uint32_t>((e + phase) * static_cast<int>(sizeof(T)));
     Granules<T>::aligned(r, [&](int i) { return ld_shared16(g + 16 * i); });
@@ -686,7 +684,7 @@ __device__ __forceinline__ void sum_staged(RowSum<T, CAP>& acc, const Stage<T, A
 }
 
 // Writes -G q over a run of `cols` columns read from global memory; the
-// one-hot columns follow.  The units of 8 columns are aligned to the gradient
+// one-hot columns follow.  The units of columns are aligned to the gradient
 // row's own 16-byte boundaries, so that odd rows are stored in whole vectors
 // too, and are read in whole vectors where the logits' row has the same phase
 // (contiguous logits), else from the two granules that hold them.  With a cap
@@ -983,8 +981,8 @@ __device__ __forceinline__ int distill_few(const LossArgs& a, int64_t row, bool 
   return n;
 }
 // More than 64: the row's other eight warps find this CTA's targets and load
-// their logits, each thread up to 4 of the k; the ninth forms the part.  (All of
-// it by the ninth warp but the reading of the ids: MEASURED.)
+// their logits, each thread up to 4 of the k; the ninth forms the part (4096 x
+// 151936 bf16 k = 1024 919 us, 1101 when the ninth did all of it).
 static_assert(VLS_MAX_TOPK <= 4 * kLossThreads, "a thread takes up to 4 targets");
 constexpr int kTargetWords = VLS_MAX_TOPK / 32;
 template <class T>
@@ -1045,9 +1043,9 @@ __device__ __forceinline__ int distill_many(int k, const Targets& t, const Scale
 }
 
 // The row's loss, G and coefficients from its C CTAs' parts; warp 0.
-__device__ __forceinline__ float distill_finish(const DistillPart* parts, int C, float M, const LogSum& ls, const Scale& S,
-                                                float inv_tau_lo, bool known, float lse, float w, DistillRow* r,
-                                                float* G) {
+__device__ __forceinline__ float distill_finish(const DistillPart* parts, int C, float M, const LogSum& ls,
+                                                const Scale& S, float inv_tau_lo, bool known, float lse, float w,
+                                                DistillRow* r, float* G) {
   const int lane = threadIdx.x & 31;
   const DistillPart d = lane < C ? parts[lane] : DistillPart{0.0f, 0.0f, 0.0f, neg_inf()};
   const float top = warp_all<true>(d.base), b = centre(top), base = centre(d.base);
@@ -1152,9 +1150,10 @@ __device__ __forceinline__ void prefetch_run(const T* run, int64_t cols) {
 
 // CTAs an SM that the registers must leave room for.  Staged rows: as many as
 // their runs leave room for in shared memory, but a distillation row at odd
-// addresses, whose ninth warp takes it over the registers (4096 x 30011 fp16: 117
-// us at 4, 120 at 5).  Streamed log-probabilities: 4096 x 151936 bf16 190 us at
-// 6, 192 at 8; at odd addresses 4096 x 30011 fp16 73 us at 5, 80 at 6, 74 at 4.
+// addresses, whose ninth warp takes it over the registers (4096 x 30011 fp16: 110
+// us at 4, 115 at 5).  Streamed log-probabilities with their pair launch: 4096 x
+// 151936 bf16 193 us at 6, 194 at 5, 196 at 8; at odd addresses 4096 x 30011 fp16
+// 64 us at 5, 68 at 6, 66 at 4.
 template <class T, int LOSS, bool CAP, bool ALIGNED>
 constexpr int loss_min_blocks() {
   if (sizeof(T) == 4) return 4;
@@ -1168,17 +1167,21 @@ constexpr int loss_min_blocks() {
 // the row from global memory.
 //
 // What bounds it, and times with the gradient (bytes: one read, one write):
-//  - aligned 16-bit rows, memory: 4096 x 151936 bf16 policy 385 us (6.5 TB/s),
-//    distillation k = 64 407 us, 18750 x 32000 bf16 policy 362 us (6.6 TB/s).
+//  - aligned 16-bit rows, memory: 4096 x 151936 bf16 policy 386 us (6.5 TB/s),
+//    distillation k = 64 405 us, 18750 x 32000 bf16 policy 363 us (6.6 TB/s).
 //    A statistics kernel and a gradient kernel in turn read the logits twice: 193
 //    + 368 us at the first of these;
-//  - fp32, memory, with 3 or 4 CTAs an SM: 2048 x 151936 policy 382 us (6.5 TB/s),
-//    1024 x 262144 407 us (5.3 TB/s);
+//  - fp32, memory, with 3 or 4 CTAs an SM: 2048 x 151936 policy 384 us (6.5 TB/s),
+//    1024 x 262144 406 us (5.3 TB/s);
 //  - rows at odd addresses, memory and issue: a unit of columns is put together
-//    from two granules: 4096 x 151937 bf16 policy 429 us (5.8 TB/s), 4096 x 30011
-//    fp16 106 us (4.6 TB/s; 98 at 30008 columns: rows of 9 waves of CTAs);
-//  - softcapped rows, issue and the special-function unit: two exponentials and
-//    a reciprocal a column and sweep; 2048 x 262144 bf16 547 us (3.9 TB/s);
+//    from two granules: 4096 x 151937 bf16 policy 431 us (5.8 TB/s);
+//  - 16-bit rows of 44 to 64 KB, latency: 3 CTAs of 8 warps fill an SM's shared
+//    memory, and neither memory (63%) nor issue (56%) is at its limit: 4096 x 30011
+//    fp16 107 us (4.6 TB/s), 30008 columns, which are aligned, 100 us;
+//  - softcapped rows, latency and issue: two exponentials and a reciprocal a column
+//    and sweep in dependent steps, the special-function unit 62% and the issue slots
+//    74% busy; 2048 x 262144 bf16 547 us (3.9 TB/s), 326 of them without the
+//    gradient;
 //  - few rows, latency (a row's chain copy, sum, cluster exchange, store): 8 x
 //    32000 bf16 7 us, 16 x 151936 k = 20 distillation 9 us, the loss's sum included.
 // One cluster a row and launch beats clusters that stay and refill their shared
