@@ -32,6 +32,12 @@ __device__ __forceinline__ bool grows(float vmax_raw, float m_raw, float m) {
   return vmax_raw > m_raw || (CAP && m == neg_inf());
 }
 
+// rescale of one of two tensors, whose max may still be -inf when the other one's
+// grows: -inf - -inf is NaN, and the smaller of NaN and 0 is 0, a factor of 1.
+__device__ __forceinline__ float rescale_side(float m_old, float m_new) {
+  return ex2(fminf((m_old - m_new) * kLog2e, 0.0f));
+}
+
 template <bool PARTIAL>
 __device__ __forceinline__ fp2 keep(fp2 e, int i, int valid) {
   if (!PARTIAL) return e;
@@ -137,7 +143,8 @@ struct KlAcc {
     if (up || uq) {
       const float Mp = up ? (CAP ? cap_zr_rare(vmp, K) : vmp) : mp;
       const float Mq = uq ? (CAP ? cap_zr_rare(vmq, K) : vmq) : mq;
-      const float fp = CAP ? rescale_rare(mp, Mp) : rescale(mp, Mp), fq = CAP ? rescale_rare(mq, Mq) : rescale(mq, Mq);
+      const float fp = CAP ? rescale_rare(mp, Mp) : rescale_side(mp, Mp);
+      const float fq = CAP ? rescale_rare(mq, Mq) : rescale_side(mq, Mq);
       const float shift = CAP ? ((mp - Mp) - (mq - Mq)) * kLog2e : (mp - Mp) - (mq - Mq);
       w2 = mp != neg_inf() ? mul2(fma2(sp2, splat(shift), w2), splat(fp)) : 0;
       sp2 = mul2(sp2, splat(fp));
@@ -209,7 +216,8 @@ struct FusedAcc {
     if (ua || ub) {
       const float Ma = ua ? (CAP ? cap_zr_rare(vma, K) : vma) : ma;
       const float Mb = ub ? (CAP ? cap_zr_rare(vmb, K) : vmb) : mb;
-      const float fa = CAP ? rescale_rare(ma, Ma) : rescale(ma, Ma), fb = CAP ? rescale_rare(mb, Mb) : rescale(mb, Mb);
+      const float fa = CAP ? rescale_rare(ma, Ma) : rescale_side(ma, Ma);
+      const float fb = CAP ? rescale_rare(mb, Mb) : rescale_side(mb, Mb);
       const float u = CAP ? kLog2e : 1.0f;   // units of W: log2 with a cap
       wh2 = ma != neg_inf() ? mul2(fma2(sa2, splat(CAP ? (ma - Ma) * kLog2e : ma - Ma), wh2), splat(fa)) : 0;
       if constexpr (DIR == kFusedKlReverse)
