@@ -127,3 +127,52 @@ def test_fused_gradient_of_a_masked_side(dtype, direction):
     ref = (oracle.logp_bwd(xa, ids.cpu().numpy(), gl.cpu().numpy()) + oracle.entropy_bwd(xa, gr.cpu().numpy())
            + oracle.kl_bwd(xa, xb, gr.cpu().numpy(), direction))
     assert_grad_close(d, ref, "fused gradient")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("v", SIZES)
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_runs_of_nan(v, dtype, cap):
+    """A NaN logit makes every statistic and gradient of its row NaN, whole
+    vectors and whole warps' shares of nothing else among them; the last row (and
+    one whose run lies behind a short row's end) is finite."""
+    a, b, ids, gk, gr = _data(v, dtype, v + 1)
+    _fill(a, float("nan"))
+    n, nan = len(a), torch.isnan(a).any(1)
+    assert nan.sum() >= n - 2 and not nan[-1]
+    H, st = B.vls_entropy_fwd(a, cap)
+    lp, sl = B.vls_logp_fwd(a, ids, -100, cap)
+    grads = [B.vls_entropy_bwd(a, gr, H, st, cap), B.vls_logp_bwd(a, ids, gk, sl, -100, cap)]
+    stats = [H, lp, st, sl]
+    for d in ("reverse", "forward"):
+        for x, y in ((a, b), (b, a)):
+            kl, sx, sy = B.vls_kl_fwd(x, y, d, cap)
+            grads.append(B.vls_kl_bwd(x, y, gr, kl, sx, sy, d, cap))
+            out = B.vls_fused_fwd(x, y, ids, direction=d, cap=cap)
+            stats += [kl, out["kl"]] + ([out["H"], out["logp"]] if x is a else [])
+    for i, s in enumerate(stats):
+        s = s.reshape(n, -1)
+        s = s[:, 1:] if i in (2, 3) else s      # (max, log-sum): the max is that of the columns that are numbers
+        assert torch.isnan(s[nan]).all() and torch.isfinite(s[~nan]).all(), i
+    for i, d in enumerate(grads):
+        assert torch.isnan(d[nan]).all() and torch.isfinite(d[~nan]).all(), i
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_runs_of_nan_sharded(dtype):
+    """A shard of nothing but NaN among finite ones."""
+    v = 30000
+    a, b, ids, *_ = _data(v, dtype, 4)
+    a[0, 10000:20000] = float("nan")
+    a[1, :10000] = float("nan")
+    a[2, 12000:12008] = float("nan")
+    bounds = ((0, 10000), (10000, 20000), (20000, v))
+    both = [B.vls_logp_partial(a[:, s:e], ids, s, v) for s, e in bounds]
+    lp, _ = B.vls_logp_combine(torch.stack([p for p, _ in both]), torch.stack([z for _, z in both]), ids, v)
+    H, _ = B.vls_entropy_combine(torch.stack([B.vls_entropy_partial(a[:, s:e]) for s, e in bounds]))
+    outs = [lp, H]
+    for d in ("reverse", "forward"):
+        for x, y in ((a, b), (b, a)):
+            outs.append(B.vls_kl_combine(torch.stack([B.vls_kl_partial(x[:, s:e], y[:, s:e], d) for s, e in bounds]), d)[0])
+    for o in outs:
+        assert torch.isnan(o[:3]).all() and torch.isfinite(o[3:]).all()

@@ -46,6 +46,15 @@ __device__ __forceinline__ fp2 keep(fp2 e, int i, int valid) {
   return pk(2 * i < valid ? a : 0.0f, 2 * i + 1 < valid ? b : 0.0f);
 }
 
+// A vector of -inf and NaN columns, while nothing finite has been seen: the
+// former weigh 0, the latter make the sum NaN.  (In a branch of its own: the same
+// through the ordinary path, with a centre of 0, cost the logp sweep 1%.)
+template <class T>
+__device__ __forceinline__ void add_masked(fp2& s, const Raw8<T>& v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = add2(s, ex2_2(v.pair(i)));
+}
+
 template <class T, bool CAP>
 struct LogpAcc {
   using State = LogpState;
@@ -73,7 +82,10 @@ struct LogpAcc {
         m = vm;
         nm2 = splat(-vm);
       }
-      if (m == neg_inf()) return;
+      if (m == neg_inf()) {
+        add_masked(s2, v);
+        return;
+      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -106,7 +118,10 @@ struct EntropyAcc {
       m = mn;
       nm2 = splat(CAP ? cap_b2(mn, K) : -mn);
     }
-    if (!CAP && m == neg_inf()) return;
+    if (!CAP && m == neg_inf()) {
+      add_masked(s2, v);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       fp2 d, e;
@@ -176,14 +191,15 @@ struct KlAcc {
         sq2 = add2(sq2, eq);
         w2 = fma2(ep, sub2(dp, dq), w2);
       }
-    } else if (p_ok || q_ok) {
-      // one side has seen only -inf so far (no W term: a finite P column
-      // against an all -inf Q run is a mismatch, already flagged); never
-      // with a cap, where no logit stays -inf
+    } else {
+      // a side has seen nothing finite so far (no W term: a finite P column
+      // against an all -inf Q run is a mismatch, already flagged); its centre is
+      // 0, so that -inf columns weigh 0 and NaN reach the sum; never with a cap,
+      // where no logit stays -inf
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (p_ok) sp2 = add2(sp2, keep<PARTIAL>(ex2_2(mul2(add2(v.pair_clamped(i), nmp2), splat(kLog2e))), i, valid));
-        if (q_ok) sq2 = add2(sq2, keep<PARTIAL>(ex2_2(mul2(add2(q.pair_clamped(i), nmq2), splat(kLog2e))), i, valid));
+        sp2 = add2(sp2, keep<PARTIAL>(ex2_2(mul2(add2(v.pair_clamped(i), nmp2), splat(kLog2e))), i, valid));
+        sq2 = add2(sq2, keep<PARTIAL>(ex2_2(mul2(add2(q.pair_clamped(i), nmq2), splat(kLog2e))), i, valid));
       }
     }
   }
@@ -261,10 +277,12 @@ struct FusedAcc {
           else wk2 = fma2(eb, sub2(db, da), wk2);
         }
       }
-    } else if (a_ok || b_ok) {
-      // one side has seen only -inf so far: no cross term (a finite column
+    } else {
+      // a side has seen nothing finite so far: no cross term (a finite column
       // of the KL's first argument against an all -inf run is flagged);
       // never with a cap
+      if (!a_ok) add_masked(sa2, v);
+      if (kHasB && !b_ok) add_masked(sb2, q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (a_ok) {

@@ -598,7 +598,7 @@ struct LogpState {
   __device__ static LogpState identity() { return {neg_inf(), 0.0f}; }
   __device__ static LogpState combine(const LogpState& a, const LogpState& b) {
     const float M = fmaxf(a.m, b.m);
-    if (M == neg_inf()) return identity();
+    if (M == neg_inf()) return {M, a.s + b.s};   // 0, or the NaN of one of them
     return {M, a.s * rescale(a.m, M) + b.s * rescale(b.m, M)};
   }
   __device__ LogpState shfl_xor(int lane_mask) const {
@@ -611,7 +611,7 @@ struct EntropyState {
   __device__ static EntropyState identity() { return {neg_inf(), 0.0f, 0.0f}; }
   __device__ static EntropyState combine(const EntropyState& a, const EntropyState& b) {
     const float M = fmaxf(a.m, b.m);
-    if (M == neg_inf()) return identity();
+    if (M == neg_inf()) return {M, a.s + b.s, 0.0f};
     const float fa = rescale(a.m, M), fb = rescale(b.m, M);
     const float wa = a.m != neg_inf() ? fa * fmaf(a.s, a.m - M, a.w) : 0.0f;
     const float wb = b.m != neg_inf() ? fb * fmaf(b.s, b.m - M, b.w) : 0.0f;
