@@ -176,3 +176,24 @@ def test_runs_of_nan_sharded(dtype):
             outs.append(B.vls_kl_combine(torch.stack([B.vls_kl_partial(x[:, s:e], y[:, s:e], d) for s, e in bounds]), d)[0])
     for o in outs:
         assert torch.isnan(o[:3]).all() and torch.isfinite(o[3:]).all()
+
+
+@pytest.mark.parametrize("start,end", [(0, 32), (0, 64), (32, 96), (0, 2048), (2048, 2100), (3, 2990)])
+def test_linear_head_runs_of_nan(start, end):
+    """Rows of the head's weight that are NaN make their columns NaN, and with them
+    every row's statistics, whatever run of columns they fill."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    h = torch.randn((130, 72), generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randn((3000, 72), generator=g, device=DEV).to(torch.bfloat16)
+    ids = torch.full((130, 1), 2999, device=DEV)
+    base, _, _ = B.vls_linear_logp_fwd(h, w, ids)
+    assert torch.isfinite(base).all()
+    w[start:end] = float("nan")
+    lp, st, status = B.vls_linear_logp_fwd(h, w, ids)
+    lp2, _, status2 = B.vls_linear_logp_fwd_noalloc(h, w, ids)
+    assert int(status.item()) == 0 and int(status2.item()) == 0
+    assert torch.isnan(lp).all() and torch.isnan(lp2).all() and torch.isnan(st[:, 1]).all()
+    one = h.clone()
+    one[5] = float("nan")
+    lp, _, _ = B.vls_linear_logp_fwd(one, torch.nan_to_num(w), ids)
+    assert torch.isnan(lp[5]).all() and torch.isfinite(lp[:5]).all() and torch.isfinite(lp[6:]).all()

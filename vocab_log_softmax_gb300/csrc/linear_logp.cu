@@ -54,6 +54,10 @@ struct LogpEpi {
     float zt[kLinMaxTopk];
   };
 
+  // 0 while nothing finite has been seen: -inf columns weigh 0, and columns of
+  // nothing but NaN still make the sum NaN
+  __device__ static float centre(float m) { return m > dev::neg_inf() ? m : 0.0f; }
+
   __device__ State begin(int64_t row, bool row_ok, int) const {
     State st;
     st.m = dev::neg_inf();
@@ -76,10 +80,10 @@ struct LogpEpi {
       for (int i = 1; i < 31; i += 2) cmax = dev::max3(cmax, v[i], v[i + 1]);
       cmax = fmaxf(cmax, v[31]);
       if (cmax > st.m) {
-        st.s = st.m == dev::neg_inf() ? 0.0f : st.s * dev::ex2((st.m - cmax) * dev::kLog2e);
+        st.s *= dev::ex2((st.m - cmax) * dev::kLog2e);   // times 0 the first time; NaN stays
         st.m = cmax;
       }
-      const dev::fp2 m2 = dev::splat(st.m), l2 = dev::splat(dev::kLog2e);
+      const dev::fp2 m2 = dev::splat(centre(st.m)), l2 = dev::splat(dev::kLog2e);
       dev::fp2 acc = dev::splat(0.0f);
 #pragma unroll
       for (int i = 0; i < 32; i += 2)
@@ -89,11 +93,11 @@ struct LogpEpi {
 #pragma unroll
       for (int i = 0; i < 32; ++i) cmax = i < nvalid ? fmaxf(cmax, v[i]) : cmax;
       if (cmax > st.m) {
-        st.s = st.m == dev::neg_inf() ? 0.0f : st.s * dev::ex2((st.m - cmax) * dev::kLog2e);
+        st.s *= dev::ex2((st.m - cmax) * dev::kLog2e);   // times 0 the first time; NaN stays
         st.m = cmax;
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) cs += i < nvalid ? dev::ex2((v[i] - st.m) * dev::kLog2e) : 0.0f;
+      for (int i = 0; i < 32; ++i) cs += i < nvalid ? dev::ex2((v[i] - centre(st.m)) * dev::kLog2e) : 0.0f;
     }
     st.s += cs;
 #pragma unroll
