@@ -1,5 +1,4 @@
-"""One call of each training loss with its gradient, for a profiler: the
-cases of losses_ncu.md.  Run from the repository's root."""
+"""One call of each training loss with its gradient, for a profiler to record."""
 
 import os
 import sys
